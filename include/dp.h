@@ -630,9 +630,10 @@ int dp_osdn_bwd_bf16(const void* q, const void* k, const void* v, const float* b
  * All tensor pointers and states 16-byte aligned; no other output overlaps an input.
  * Computed in chunks of 64 tokens
  * (fp32 inputs: 32) with fp32 states, scores and sums; on the bf16 path computed
- * MFMA operands are split into two or three bf16 terms, so the only rounding to
- * fewer bits is that of the result, and the range is bf16's (fp32's), less 2^40 for
- * what is held in between (states below 2^87 in magnitude).  A value v
+ * MFMA operands are split into three bf16 terms (24 bits), so the only rounding to
+ * fewer bits is that of the result (a bf16 out is the DP_OUT_F32 one rounded), and the
+ * range is bf16's (fp32's), less 2^40 for what is held in between (states below 2^87
+ * in magnitude).  A value v
  * that is not finite makes its head's outputs not finite from the start of its
  * chunk on; other heads and sequences are unaffected.
  * Errors: DP_EINVAL (null required pointer, misalignment, sizes <= 0, H not a

@@ -44,18 +44,15 @@
 // (a difference of two of them is an exponent, and a chunk with strong decays
 // has large sums).  On the bf16 path the inputs are MFMA operands as they are.
 // Computed operands (scores, the state where it is read, the weighted values that
-// build it) are split into bf16 terms, x = h + m (+ l) with h = bf16(x), m = bf16(x - h),
-// l = bf16(x - h - m), one MFMA per term.  One term alone would leave an error of 2^-9
-// per operand, as large as the rounding of the bf16 result itself; two leave 2^-18 at
-// most, three 24 bits.  The values that build the state take three: it is an fp32 result
-// (with two its error against fp64 rises from 1.3e-7 to over 1e-6, for 3 us of 128).
-// Scores and the state that is read take two where the result is bf16, and three where
-// it is fp32 (DP_OUT_F32).  With the gradient of the decays, an fp32 result too, dq and dk
-// take three throughout: a and b are summed over a segment, r and c over a chunk (B = 4,
-// H = 16, L = 4096, d = 128: dl's error against fp64 7e-7 in 371 us, with two-term scores
-// 1e-6 in 365, with two-term states as well 6.5e-6 for 15 us less; short sequences 2e-7
-// against 2e-6 with two-term scores, 145 against 127 us at B = 32, H = 16, L = 512,
-// d = 64).  The fp32 path runs fp32 MFMA.
+// build it) are split into three bf16 terms, x = h + m + l with h = bf16(x), m = bf16(x - h),
+// l = bf16(x - h - m), one MFMA per term: 24 bits, so that the only rounding to fewer is
+// the result's, and a result's bits do not depend on which others are asked for.  Two
+// terms (17 bits) are quicker (B = 4, H = 16, L = 4096, d = 128: forward 114 against 122
+// us, gradient 355 against 383, without the decays' gradient 280 against 330) and leave a
+// bf16 result's error against fp64 where it is, 1.66e-3 of its size; but 0.2% of the
+// elements then round otherwise than the fp32 value (of a forward at that size; three terms:
+// 0.02%, as many as another order of the sums), and the fp32 results (states, decays'
+// gradient) are off by 1e-6 to 7e-6.  The fp32 path runs fp32 MFMA.
 #pragma once
 
 #include <atomic>
@@ -95,8 +92,8 @@ struct LaOp;
 template <>
 struct LaOp<bf16_t> {
   using frag_t = bf16x8_t;
-  static constexpr int C = 64;        // tokens per chunk
-  static constexpr int STATE_NS = 3;  // terms of the values that build the state
+  static constexpr int C = 64;  // tokens per chunk
+  static constexpr int NS = 3;  // terms of a computed operand
   static constexpr int pitch(int d) { return d < 32 ? 32 : d; }
   // block 0 of row r, in elements, for rows of `ld` elements (16 / CH rows span the banks)
   __device__ __forceinline__ static int swz(int r, int ld) {
@@ -214,7 +211,7 @@ template <>
 struct LaOp<float> {
   using frag_t = f32x8_t;
   static constexpr int C = 32;  // half the scores per token: fp32 MFMA is the bound
-  static constexpr int STATE_NS = 1;
+  static constexpr int NS = 1;
   static constexpr int pitch(int d) { return (d < 32 ? 32 : d) + 4; }
   __device__ __forceinline__ static int at(int r, int c4, int ld) { return r * ld + 4 * c4; }
   __device__ __forceinline__ static void put16(float* s, int r, int c4, int ld, const u32x4_t& v) { st16(s + at(r, c4, ld), v); }
@@ -523,11 +520,11 @@ constexpr int la_waves(int dv, int nw) { return dv / 16 < nw ? dv / 16 : nw; }
 // tiles: A = b transposed, B = the weighted values split into terms.  The decay stays in
 // a factor (the state is scale x) and the weights are divided by it, so that a chunk
 // multiplies 64 values a lane only where the factor has left [2^-40, 2^40] (or is NaN).
-template <typename T, int NS, int DKP, int CT, int LB, int LC>
+template <typename T, int DKP, int CT, int LB, int LC>
 __device__ __forceinline__ void la_update(f32x4_t (&x)[DKP / 16][CT], float& scale, const T* sB, const T* sC,
                                           const float* sW, float tot, int col0) {
   using Op = LaOp<T>;
-  constexpr int C = Op::C;
+  constexpr int C = Op::C, NS = Op::NS;
   const int g = (threadIdx.x >> 4) & 3;
   scale = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(scale * tot)));
   if (!(scale >= 0x1p-40f && scale <= 0x1p40f)) {
@@ -642,13 +639,11 @@ struct LaWalkArgs {
   int rev, tr, r_f32, H;
 };
 
-// Terms of the scores (NP), of the state where it is read (NS) and of the values that
-// build it (SNS: all of them where the walk ends with a state that is a result).
-template <typename T, int DK, int DV, int NP, int NS, int SNS, int NW>
+template <typename T, int DK, int DV, int NW>
 struct LaWalk {
   using Op = LaOp<T>;
   using frag_t = typename Op::frag_t;
-  static constexpr int C = Op::C, R = C / 16;
+  static constexpr int C = Op::C, R = C / 16, NS = Op::NS;
   static constexpr int DKP = DK < 32 ? 32 : DK;
   static constexpr int WV = la_waves(DV, NW);  // wavefronts that hold columns
   static constexpr int CT = DV / 16 / WV;      // column tiles of each
@@ -658,9 +653,9 @@ struct LaWalk {
   static constexpr int oB = oA + C * LA * (int)sizeof(T);
   static constexpr int oC = oB + C * LA * (int)sizeof(T);
   static constexpr int oP = oC + C * LC * (int)sizeof(T);
-  static constexpr int oG = oP + NP * C * LP * (int)sizeof(T);
+  static constexpr int oG = oP + NS * C * LP * (int)sizeof(T);
   static constexpr int oDot = oG + 4 * LaDecayRing<C>::BYTES;
-  static constexpr int LDS = oDot + WV * C * 8;
+  static constexpr int LDS = oDot, LDS_DOTS = oDot + WV * C * 8;  // without and with products (`dots`)
 
   __device__ __forceinline__ static void run(const LaWalkArgs& p, char* lds, long long row0, int len, int h) {
     T* sA = reinterpret_cast<T*>(lds + oA);
@@ -780,7 +775,7 @@ struct LaWalk {
           const float v = sc[u][e] * __builtin_amdgcn_exp2f(d);
           sc[u][e] = (rev ? e >= edge : e <= edge) ? v : 0.f;
         }
-        Op::template put<NP>(sP + 16 * rt[u] * LP + Op::pcol_step(rp0, ct[u]), C * LP, sc[u]);
+        Op::template put<NS>(sP + 16 * rt[u] * LP + Op::pcol_step(rp0, ct[u]), C * LP, sc[u]);
       }
 
       // the state's part of the result, transposed (lane: token n, columns 4g..4g+3)
@@ -831,7 +826,7 @@ struct LaWalk {
           for (int r = 0; r < R; ++r) {
             if (rev ? ks < r / 2 : ks > r / 2) continue;
 #pragma unroll
-            for (int s = 0; s < NP; ++s) {
+            for (int s = 0; s < NS; ++s) {
               const frag_t pf = Op::prow(sP + s * C * LP + 16 * r * LP, Op::row_step(rp0, ks));
 #pragma unroll
               for (int t = 0; t < CT; ++t) acc[r][t] = Op::mma(vf[t], pf, acc[r][t]);
@@ -859,7 +854,7 @@ struct LaWalk {
           }
         }
         if (it + 1 < nc || p.x1 != nullptr)
-          la_update<T, SNS, DKP, CT, LA, LC>(x, scale, sB, sC, rev ? dec.E : dec.W, *dec.tot, col0);
+          la_update<T, DKP, CT, LA, LC>(x, scale, sB, sC, rev ? dec.E : dec.W, *dec.tot, col0);
       }
       block_sync_lds();
       if (p.dots != nullptr && tid < C && tid < m) {
@@ -960,7 +955,7 @@ __global__ __launch_bounds__(64 * la_fwd_waves(DV), la_fwd_waves(DV) / 2) void d
     if (it + 1 < nc) fetch(ring.chunk(it + 1));
     const LaDecays<C> dec = ring.at(it);
     total += dec.G[C - 1];
-    if (active) la_update<T, Op::STATE_NS, DKP, CT, LB, LC>(x, scale, sB, sC, rev ? dec.E : dec.W, *dec.tot, col0);
+    if (active) la_update<T, DKP, CT, LB, LC>(x, scale, sB, sC, rev ? dec.E : dec.W, *dec.tot, col0);
     block_sync_lds();
   }
   float* dst = (rev ? p.rt : p.st) + ((long long)(rev ? s - 1 : s + 1) * p.H + h) * DK * DV;
@@ -1000,13 +995,11 @@ __device__ __forceinline__ void la_end(const LaArgs& p, const LaSeg& sg, int s, 
 }
 
 // The forward walk: one workgroup per segment and head.  B = 4, H = 16, L = 4096, d = 128:
-// 92 us of the call's 118, 16 chunks a workgroup; bound by the issue of its products (44
-// GFLOP with the terms, 35 us at the 1.27 PFLOP/s of a large library product) and of the
+// the call takes 122 us, 16 chunks a workgroup; bound by the issue of its products (64
+// GFLOP with the terms, 51 us at the 1.27 PFLOP/s of a large library product) and of the
 // exponentials, splits and LDS reads between them, which overlap in part.
-template <typename T, int DK, int DV, int NS>
+template <typename T, int DK, int DV>
 __global__ __launch_bounds__(64 * la_fwd_waves(DV), 2) void dp_la_fwd_kernel(LaArgs p) {
-  constexpr int NW = la_fwd_waves(DV);
-  using W = LaWalk<T, DK, DV, NS, NS, LaOp<T>::STATE_NS, NW>;
   extern __shared__ __align__(16) char lds[];
   int s, h;
   la_block(blockIdx.x, p.geo, p.H, p.Hk, &s, &h);
@@ -1024,22 +1017,15 @@ __global__ __launch_bounds__(64 * la_fwd_waves(DV), 2) void dp_la_fwd_kernel(LaA
   w.H = p.H;
   la_start(p, sg, s, h, per, w);
   w.x1 = sg.last && p.fstate != nullptr ? p.fstate + so : nullptr;
-  if (w.x1 != nullptr)
-    W::run(w, lds, sg.row, sg.len, h);
-  else
-    LaWalk<T, DK, DV, NS, NS, NS, NW>::run(w, lds, sg.row, sg.len, h);
+  LaWalk<T, DK, DV, la_fwd_waves(DV)>::run(w, lds, sg.row, sg.len, h);
 }
 
 // The gradient's walks, one workgroup per segment, head and role: dq (forwards
-// over the transposed state), dk (backwards, transposed) and dv (backwards).  NS: terms
-// of every computed operand of dq and dk.  B = 4, H = 16, L = 4096, d = 128, with the
-// decays' gradient: 280 us of the call's 371 (states 64, scan 10, dl 15), bound as the
-// forward: 224 GFLOP in all, 177 us at that rate.
-template <typename T, int DK, int DV, int NS>
+// over the transposed state), dk (backwards, transposed) and dv (backwards).  B = 4, H =
+// 16, L = 4096, d = 128, with the decays' gradient: the call takes 383 us, bound as the
+// forward: 245 GFLOP in all, 193 us at that rate.
+template <typename T, int DK, int DV>
 __global__ __launch_bounds__(64 * kLaBwdWaves, 2) void dp_la_bwd_kernel(LaArgs p) {
-  constexpr int N = sizeof(T) == 2 ? 2 : 1;  // terms where no dl depends on them
-  using WQ = LaWalk<T, DV, DK, NS, NS, NS, kLaBwdWaves>;
-  using WV = LaWalk<T, DK, DV, N, N, N, kLaBwdWaves>;
   extern __shared__ __align__(16) char lds[];
   int s, h;
   la_block(blockIdx.x, p.geo, p.H, p.Hk, &s, &h);
@@ -1074,16 +1060,10 @@ __global__ __launch_bounds__(64 * kLaBwdWaves, 2) void dp_la_bwd_kernel(LaArgs p
     w.dot = role == 0 ? q : k;
     w.dots = role == 0 ? p.xq : p.xk;
   }
-  if (w.x1 != nullptr) {
-    LaWalk<T, DK, DV, N, N, LaOp<T>::STATE_NS, kLaBwdWaves>::run(w, lds, sg.row, sg.len, h);
-  } else if constexpr (DK == DV && NS == N) {
-    WQ::run(w, lds, sg.row, sg.len, h);
-  } else {
-    if (role == 2)
-      WV::run(w, lds, sg.row, sg.len, h);
-    else
-      WQ::run(w, lds, sg.row, sg.len, h);
-  }
+  if (DK != DV && role == 2)
+    LaWalk<T, DK, DV, kLaBwdWaves>::run(w, lds, sg.row, sg.len, h);
+  else
+    LaWalk<T, DV, DK, kLaBwdWaves>::run(w, lds, sg.row, sg.len, h);
 }
 
 // ------------------------------------------------------------ launches
@@ -1108,23 +1088,21 @@ hipError_t la_states_launch(const LaArgs& a, int roles, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename T, int DK, int DV, int NS>
+template <typename T, int DK, int DV>
 hipError_t la_fwd_launch(const LaArgs& a, hipStream_t st) {
-  using W = LaWalk<T, DK, DV, NS, NS, NS, la_fwd_waves(DV)>;
+  using W = LaWalk<T, DK, DV, la_fwd_waves(DV)>;
   static std::atomic<uint64_t> seen{0};
-  la_allow_lds(reinterpret_cast<const void*>(&dp_la_fwd_kernel<T, DK, DV, NS>), seen);
-  hipLaunchKernelGGL((dp_la_fwd_kernel<T, DK, DV, NS>), dim3((unsigned)(a.geo.nwork * a.H)), dim3(W::NT), W::LDS, st,
-                     a);
+  la_allow_lds(reinterpret_cast<const void*>(&dp_la_fwd_kernel<T, DK, DV>), seen);
+  hipLaunchKernelGGL((dp_la_fwd_kernel<T, DK, DV>), dim3((unsigned)(a.geo.nwork * a.H)), dim3(W::NT), W::LDS, st, a);
   return hipGetLastError();
 }
 
-template <typename T, int DK, int DV, int NS>
+template <typename T, int DK, int DV>
 hipError_t la_bwd_launch(const LaArgs& a, hipStream_t st) {
-  constexpr int N = sizeof(T) == 2 ? 2 : 1;
-  constexpr int l0 = LaWalk<T, DV, DK, NS, NS, NS, kLaBwdWaves>::LDS, l1 = LaWalk<T, DK, DV, N, N, N, kLaBwdWaves>::LDS;
+  constexpr int l0 = LaWalk<T, DV, DK, kLaBwdWaves>::LDS_DOTS, l1 = LaWalk<T, DK, DV, kLaBwdWaves>::LDS;
   static std::atomic<uint64_t> seen{0};
-  la_allow_lds(reinterpret_cast<const void*>(&dp_la_bwd_kernel<T, DK, DV, NS>), seen);
-  hipLaunchKernelGGL((dp_la_bwd_kernel<T, DK, DV, NS>), dim3((unsigned)(a.geo.nwork * a.H), 3), dim3(64 * kLaBwdWaves),
+  la_allow_lds(reinterpret_cast<const void*>(&dp_la_bwd_kernel<T, DK, DV>), seen);
+  hipLaunchKernelGGL((dp_la_bwd_kernel<T, DK, DV>), dim3((unsigned)(a.geo.nwork * a.H), 3), dim3(64 * kLaBwdWaves),
                      l0 > l1 ? l0 : l1, st, a);
   return hipGetLastError();
 }
@@ -1132,29 +1110,24 @@ hipError_t la_bwd_launch(const LaArgs& a, hipStream_t st) {
 enum LaStage { kLaStates, kLaFwd, kLaBwd };
 
 // One launch of a forward or gradient: `roles` for kLaStates (1: states, 2: and
-// state gradients); terms: 2 or 3 (bf16; the fp32 path has one).
+// state gradients).
 template <typename T, int DK, int DV>
-hipError_t la_stage(LaStage stage, const LaArgs& a, int roles, int terms, hipStream_t st) {
+hipError_t la_stage(LaStage stage, const LaArgs& a, int roles, hipStream_t st) {
   if (stage == kLaStates) return la_states_launch<T, DK, DV>(a, roles, st);
-  constexpr int NS = sizeof(T) == 2 ? 2 : 1;
-  if constexpr (NS == 2) {
-    if (terms == 3) return stage == kLaFwd ? la_fwd_launch<T, DK, DV, 3>(a, st) : la_bwd_launch<T, DK, DV, 3>(a, st);
-  }
-  return stage == kLaFwd ? la_fwd_launch<T, DK, DV, NS>(a, st) : la_bwd_launch<T, DK, DV, NS>(a, st);
+  return stage == kLaFwd ? la_fwd_launch<T, DK, DV>(a, st) : la_bwd_launch<T, DK, DV>(a, st);
 }
 
 }  // namespace dp
 
 #define DP_LA_DECLARE(tn, DK) \
-  hipError_t dp_la_stage_##tn##_##DK(dp::LaStage, const dp::LaArgs&, int dv, int roles, int terms, hipStream_t);
-#define DP_LA_DEFINE(T, tn, DK)                                                                                \
-  hipError_t dp_la_stage_##tn##_##DK(dp::LaStage s, const dp::LaArgs& a, int dv, int roles, int terms,          \
-                                     hipStream_t st) {                                                         \
-    switch (dv) {                                                                                              \
-      case 16: return dp::la_stage<T, DK, 16>(s, a, roles, terms, st);                                          \
-      case 32: return dp::la_stage<T, DK, 32>(s, a, roles, terms, st);                                          \
-      case 64: return dp::la_stage<T, DK, 64>(s, a, roles, terms, st);                                          \
-      case 128: return dp::la_stage<T, DK, 128>(s, a, roles, terms, st);                                        \
-    }                                                                                                          \
-    return hipErrorInvalidValue;                                                                               \
+  hipError_t dp_la_stage_##tn##_##DK(dp::LaStage, const dp::LaArgs&, int dv, int roles, hipStream_t);
+#define DP_LA_DEFINE(T, tn, DK)                                                                              \
+  hipError_t dp_la_stage_##tn##_##DK(dp::LaStage s, const dp::LaArgs& a, int dv, int roles, hipStream_t st) { \
+    switch (dv) {                                                                                            \
+      case 16: return dp::la_stage<T, DK, 16>(s, a, roles, st);                                              \
+      case 32: return dp::la_stage<T, DK, 32>(s, a, roles, st);                                              \
+      case 64: return dp::la_stage<T, DK, 64>(s, a, roles, st);                                              \
+      case 128: return dp::la_stage<T, DK, 128>(s, a, roles, st);                                            \
+    }                                                                                                        \
+    return hipErrorInvalidValue;                                                                             \
   }

@@ -131,20 +131,20 @@ LaWs layout(const LaShape& s, const dp::LaGeo& g, int single, bool bwd) {
   return w;
 }
 
-hipError_t stage(int elem, dp::LaStage st, const dp::LaArgs& a, int dk, int dv, int roles, int terms, hipStream_t str) {
+hipError_t stage(int elem, dp::LaStage st, const dp::LaArgs& a, int dk, int dv, int roles, hipStream_t str) {
   if (elem == 4) {
     switch (dk) {
-      case 16: return dp_la_stage_f32_16(st, a, dv, roles, terms, str);
-      case 32: return dp_la_stage_f32_32(st, a, dv, roles, terms, str);
-      case 64: return dp_la_stage_f32_64(st, a, dv, roles, terms, str);
-      case 128: return dp_la_stage_f32_128(st, a, dv, roles, terms, str);
+      case 16: return dp_la_stage_f32_16(st, a, dv, roles, str);
+      case 32: return dp_la_stage_f32_32(st, a, dv, roles, str);
+      case 64: return dp_la_stage_f32_64(st, a, dv, roles, str);
+      case 128: return dp_la_stage_f32_128(st, a, dv, roles, str);
     }
   } else {
     switch (dk) {
-      case 16: return dp_la_stage_bf16_16(st, a, dv, roles, terms, str);
-      case 32: return dp_la_stage_bf16_32(st, a, dv, roles, terms, str);
-      case 64: return dp_la_stage_bf16_64(st, a, dv, roles, terms, str);
-      case 128: return dp_la_stage_bf16_128(st, a, dv, roles, terms, str);
+      case 16: return dp_la_stage_bf16_16(st, a, dv, roles, str);
+      case 32: return dp_la_stage_bf16_32(st, a, dv, roles, str);
+      case 64: return dp_la_stage_bf16_64(st, a, dv, roles, str);
+      case 128: return dp_la_stage_bf16_128(st, a, dv, roles, str);
     }
   }
   return hipErrorInvalidValue;
@@ -161,7 +161,7 @@ hipError_t front(int elem, const LaShape& s, const dp::LaArgs& a, int single, in
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (single) return e;
-  if ((e = stage(elem, dp::kLaStates, a, s.dk, s.dv, roles, 0, st)) != hipSuccess || a.sum_in_walk) return e;
+  if ((e = stage(elem, dp::kLaStates, a, s.dk, s.dv, roles, st)) != hipSuccess || a.sum_in_walk) return e;
   const int per = s.dk * s.dv;
   hipLaunchKernelGGL(dp::dp_la_scan_kernel, dim3((unsigned)(s.B * s.H), (per / 4 + 255) / 256, roles), dim3(256), 0, st, a,
                      per);
@@ -215,7 +215,7 @@ int la_fwd(int elem, const void* q, const void* k, const void* v, const float* l
   a.h0_in_st = !single && h0 != nullptr && h0 == fstate;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   hipError_t e = front(elem, s, a, single, 1, st);
-  if (e == hipSuccess) e = stage(elem, dp::kLaFwd, a, dk, dv, 0, a.out_f32 ? 3 : 2, st);
+  if (e == hipSuccess) e = stage(elem, dp::kLaFwd, a, dk, dv, 0, st);
   return status(e);
 }
 
@@ -280,7 +280,7 @@ int la_bwd(int elem, const void* q, const void* k, const void* v, const float* l
   a.sum_in_walk = !single && segments(L, a.geo.seg) <= kSumInBwd;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   hipError_t e = front(elem, s, a, single, 2, st);
-  if (e == hipSuccess) e = stage(elem, dp::kLaBwd, a, dk, dv, 0, dld != nullptr ? 3 : 2, st);
+  if (e == hipSuccess) e = stage(elem, dp::kLaBwd, a, dk, dv, 0, st);
   if (e == hipSuccess && dld != nullptr) {
     const dim3 grid((unsigned)(a.geo.nwork * H));
     if (elem == 4)

@@ -320,6 +320,45 @@ def test_fp32_out_of_bf16_inputs():
     check("state", fs, rs)
 
 
+# B, H, Hk, L, dk, dv, lens: one segment, several, packed and grouped
+ASKED = [(2, 2, 1, 200, 64, 64, None), (1, 2, 2, 1500, 128, 128, None), (1, 3, 3, 700, 32, 128, None),
+         (3, 4, 2, 1300, 128, 64, [900, 0, 400])]
+
+
+@pytest.mark.parametrize("case", ASKED, ids=[f"B{c[0]}H{c[1]}L{c[3]}d{c[4]}x{c[5]}" for c in ASKED])
+def test_results_do_not_depend_on_what_else_is_asked_for(case):
+    """A bf16 result is the fp32 one rounded once: out is DP_OUT_F32's out rounded, with
+    and without the final state, and dq, dk, dv have the same bits with and without the
+    gradients of the decays and of the initial state."""
+    B, H, Hk, L, dk, dv, lens = case
+    x = make(B, H, Hk, L, dk, dv, "bf16", "token", 59, lens=lens)
+    out, fs = run_fwd(x)
+    full, fs32 = run_fwd(x, out_dtype=torch.float32)
+    alone, none = run_fwd(x, return_state=False)
+    assert none is None and torch.equal(out, full.bfloat16()) and torch.equal(out, alone) and torch.equal(fs, fs32)
+    g = run_bwd(x)
+    for left in (["ld"], ["h0"], ["ld", "h0"]):
+        part = run_bwd(x, grads={n: None for n in left})
+        assert all(torch.equal(g[n], part[n]) for n in g if n not in left), left
+
+
+@pytest.mark.parametrize("case", ASKED, ids=[f"B{c[0]}H{c[1]}L{c[3]}d{c[4]}x{c[5]}" for c in ASKED])
+def test_bf16_results_are_rounded_fp32_results(case):
+    """Element by element at most half a bf16 step off the definition, and an fp32
+    result's error: 64 * 2^-24 of the tensor's RMS (64 sums of 2^-24 of a partial sum each,
+    see the top; two-term operands would leave 2^-18 of every product)."""
+    B, H, Hk, L, dk, dv, lens = case
+    x = make(B, H, Hk, L, dk, dv, "bf16", "token", 61, lens=lens)
+    out, _ = run_fwd(x)
+    g = run_bwd(x)
+    ro, _, rg = reference(x, bwd=True)
+    for n, got, ref in [("out", out, ro)] + [(n, g[n], rg[n]) for n in "qkv"]:
+        half = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(ref), 1e-30))) - 8)
+        over = np.max(np.abs(f64(got) - ref) - half) / np.sqrt(np.mean(ref * ref))
+        say(f"  {n}: {over:.2e} of the RMS past half a step")
+        assert over <= 64 * 2.0 ** -24, n
+
+
 def test_large_and_small_values():
     """The bf16 path has bf16's range: values far outside fp16's."""
     for scale in (1e8, 1e-8):
