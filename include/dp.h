@@ -612,7 +612,8 @@ int dp_osdn_bwd_bf16(const void* q, const void* k, const void* v, const float* b
  *   ld    [B, L, H]      f32   log decay (natural logarithm) of each token and head,
  *                              at most 0 in ordinary use; [H] with DP_LA_HEAD_DECAY
  *                              (one for all tokens of a head); NULL = no decay.
- *                              -inf, and all below -1000, erases the state exactly
+ *                              -inf, and all from -1000 down, erases a finite state
+ *                              exactly
  *   out   [B, L, H, dv]    T   written (float32 with DP_OUT_F32)
  *   final_state, h0 [B, H, dk, dv] f32, each nullable; MAY be the same buffer
  *   cu_seqlens  NULL: B sequences of L tokens.  Else int32 [B + 1] in DEVICE memory:
@@ -663,7 +664,10 @@ int dp_la_fwd_bf16(const void* q, const void* k, const void* v, const float* ld,
  *                                share it, in fp32, and rounded once
  *   dv_out [B, L, H, dv]   T     written
  *   dld    [B, L, H] f32 ([H] with DP_LA_HEAD_DECAY: summed over all tokens), or
- *                                NULL (not returned); needs ld
+ *                                NULL (not returned); needs ld.  Zero where ld <= -1000
+ *                                erases the state; else exact to fp32 rounding of the
+ *                                q . dq and k . dk around the token, not of itself: a
+ *                                strong decay's tiny gradient can be less than that
  *   dh0    [B, H, dk, dv]  f32   written, or NULL
  * Packed batches: the gradients of rows behind the last sequence are zero.
  * Sums run in a fixed order: the same call gives the same bits.  Nothing from a

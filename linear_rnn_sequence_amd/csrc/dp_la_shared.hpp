@@ -121,8 +121,9 @@ static __global__ __launch_bounds__(256) void dp_la_scan_kernel(LaArgs p, int pe
 
 // dl of one segment and head (see the head of dp_la.hpp): <S, D> at the segment's start,
 // plus the sums of b - a from there to before the token, plus the suffix sums of r - c
-// inside the token's chunk of C, all in fp64.  With one decay per head the segment's sum
-// of dl goes to ldpart.
+// inside the token's chunk of C, all in fp64.  A decay that erases the state has gradient
+// zero (the difference of the sums would leave their rounding).  With one decay per head
+// the segment's sum of dl goes to ldpart.
 constexpr int kDldThreads = 512;
 template <int C>
 __global__ __launch_bounds__(kDldThreads) void dp_la_dld_kernel(LaArgs p, int per) {
@@ -157,16 +158,19 @@ __global__ __launch_bounds__(kDldThreads) void dp_la_dld_kernel(LaArgs p, int pe
     return x;
   };
   // the first tokens' terms on the way meanwhile
-  auto fetch = [&](int e, float2& q, float2& k) {
+  float2 q, k;
+  float ld;
+  auto fetch = [&](int e) {
     const int i = e + tid;
     q = k = float2{0.f, 0.f};
+    ld = 0.f;
     if (i < sg.len) {
       q = p.xq[(sg.row + i) * p.H + h];
       k = p.xk[(sg.row + i) * p.H + h];
+      ld = p.ld_head ? p.ld[h] : p.ld[(sg.row + i) * p.H + h];
     }
   };
-  float2 q, k;
-  fetch(0, q, k);
+  fetch(0);
   double f = 0.0;
   auto dot = [&](const f32x4_t& a, const f32x4_t& b) {
     f += (double)(a[0] * b[0] + a[1] * b[1]) + (double)(a[2] * b[2] + a[3] * b[3]);
@@ -197,7 +201,8 @@ __global__ __launch_bounds__(kDldThreads) void dp_la_dld_kernel(LaArgs p, int pe
   for (int w = 0; w < NW; ++w) carry += red[w];
   for (int e = 0; e < sg.len; e += NT) {
     const double cross = (double)k.x - (double)q.x, in = (double)q.y - (double)k.y;
-    if (e + NT < sg.len) fetch(e + NT, q, k);
+    const bool erases = ld <= kLaMinLog;
+    if (e + NT < sg.len) fetch(e + NT);
     const double cc = la_scan64(cross), ci = la_scan64(in);
     if (l == 63) run[wave] = cc;
     // the chunk's total of r - c: lane 63's, or for chunks of 32 lane 31's and the rest
@@ -208,7 +213,7 @@ __global__ __launch_bounds__(kDldThreads) void dp_la_dld_kernel(LaArgs p, int pe
     for (int w = 0; w < wave; ++w) before += run[w];
     const int i = e + tid;
     if (i < sg.len) {
-      const double d = before + suffix;
+      const double d = erases ? 0.0 : before + suffix;
       sum += d;
       if (!p.ld_head) p.dld[(sg.row + i) * p.H + h] = (float)d;
     }

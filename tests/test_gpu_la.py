@@ -261,6 +261,33 @@ def test_resets_and_infinite_decays(dtype):
     assert float(g["ld"][0, [70, 128]].abs().max()) <= 40 * F32_TOL * float(g["ld"].abs().max())
 
 
+# B, H, L, decay, lens, tokens whose decay erases the state: the first and the last, chunk
+# borders of either path, neighbours, in one segment and in many, packed, a whole head
+ERASED = [(2, 2, 200, "token", None, [0, 31, 32, 63, 64, 65, 128, 199]), (1, 1, 2500, "token", None, [5, 640, 641, 2499]),
+          (3, 2, 400, "token", [250, 0, 150], [0, 100, 249, 250, 399]), (2, 3, 300, "head", None, None)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", ERASED, ids=["one", "many", "packed", "head"])
+def test_gradient_of_an_erasing_decay_is_zero(case, dtype):
+    """e^ld is 0 from -1000 down, and so is its derivative, exactly; the others' stays the
+    definition's."""
+    B, H, L, decay, lens, at = case
+    x = make(B, H, H, L, 64, 64, dtype, decay, 67, lens=lens)
+    if at is None:
+        x["ld"][1] = float("-inf")
+    else:
+        x["ld"][..., at, :] = float("-inf")
+        x["ld"][..., at[1], :] = -1000.0
+        x["ld"][..., at[2], 0] = -3e38
+    g = run_bwd(x)
+    zero = x["ld"] <= -1000.0
+    assert bool(zero.any()) and bool((g["ld"].cpu()[zero] == 0).all())
+    rg = reference(x, bwd=True)[2]
+    for n in ("q", "k", "v", "h0", "ld"):
+        check(n, g[n], rg[n], low=dtype == "bf16" and n in "qkv")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_gradient_against_differences(dtype):
     """Directional derivatives of the fp64 definition by central differences."""
