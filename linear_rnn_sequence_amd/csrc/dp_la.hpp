@@ -35,8 +35,8 @@
 // With one segment a single launch walks it.  With several, dp_la_states_kernel
 // sums each segment's own contribution to the state (it reads two of the
 // tensors), dp_la_scan_kernel runs the decayed prefix sum over the segments in
-// fp32, and the walks start from the result (over few segments they add them up
-// themselves: the states come from L2, and a launch is saved).  The first segment starts from the
+// fp32, and the walks start from the result (where their states are few or small they
+// add them up themselves: they come from L2, and a launch is saved).  The first segment starts from the
 // initial state and the last ends with the final one, so a sequence of one segment
 // takes no part in either.
 //

@@ -95,11 +95,26 @@ void plan_fwd(const LaShape& s, dp::LaGeo* g, int* single) {
   plan(s, dp::la_fwd_waves(s.dv) == 8 ? 256 : 512, 1, g, single);
 }
 void plan_bwd(const LaShape& s, dp::LaGeo* g, int* single) { plan(s, 256, 2, g, single); }
-// Segments of a sequence (at most) that the walks add up themselves; more of them take
-// the scan's launch, since a walk reads all that come before.  Packed rows give only a
-// bound, that one long sequence reaches: 24 there (24 sequences of 16 heads of 128 in 16384
-// rows 137 against 145 us, one long and 23 short ones 156 either way).
-constexpr int kSumInFwd = 16, kSumInPacked = 24, kSumInBwd = 3;
+// Whether the walks add up the earlier segments' states themselves or start from the scan's
+// sums, by what either costs a sequence of n segments, in microseconds (fp32 states either
+// way, so the inputs' type does not matter):
+//   scan: its launch, 4, and its chain over the segments, n / 8;
+//   walk: the longest one reads n - 1 states first, at 128 KB a microsecond (the 64 bytes
+//         a clock that a CU takes from L2); in the gradient three roles read them, two of
+//         them side by side on a CU and the decays' gradient once more: 20 KB.
+// Packed rows count half: only the bound of n is known, which one long sequence reaches,
+// and others' products run beside its reads.  Timed both ways for 1 to 64 heads of 16 to
+// 128 columns, 2 to 512 segments, one length and up to 48 packed sequences, both types and
+// directions (796 cases): on average 0.4% slower than the quicker of the two.  d = 128, one
+// length, walk against scan: 8 segments (32 heads) 66.6 / 67.4 us, 16 (16) 47.9 / 45.8, 32
+// (8) 45.6 / 38.4; d = 64: 16 (32) 33.3 / 38.0, 64 (8) 29.2 / 31.9, 512 (1) 169 / 226.  24 packed
+// sequences (d = 128, 16 heads) 139 / 144, 48 of them (43 segments, one long) 203 / 181.
+// Gradient, d = 128: 2 segments (128 heads) 354 / 355, 4 (64) 362 / 357, 8 (16) 66 / 45; d =
+// 32: 16 (16) 44.2 / 46.2, 128 (2) 97 / 89.
+bool sum_in_walk(const LaShape& s, const dp::LaGeo& g, bool bwd) {
+  const long long n = segments(s.L, g.seg), kb = (n - 1) * s.dk * s.dv * 4 / 1024;
+  return 8 * kb <= (bwd ? 20 : 128) * (s.packed ? 2 : 1) * (32 + n);
+}
 
 struct LaWs {
   size_t tab, order, st, rt, sdec, rdec, xq, xk, dh0, ldpart, pq, pk, total;
@@ -209,7 +224,7 @@ int la_fwd(int elem, const void* q, const void* k, const void* v, const float* l
   a.Hk = Hk;
   a.ld_head = (flags & DP_LA_HEAD_DECAY) != 0;
   a.out_f32 = f32_out;
-  a.sum_in_walk = !single && segments(L, a.geo.seg) <= (s.packed ? kSumInPacked : kSumInFwd);
+  a.sum_in_walk = !single && sum_in_walk(s, a.geo, false);
   // In one buffer, a sequence's last segment could write the state before another has
   // started from it (the XCDs take their workgroups each at its own pace).
   a.h0_in_st = !single && h0 != nullptr && h0 == fstate;
@@ -277,7 +292,7 @@ int la_bwd(int elem, const void* q, const void* k, const void* v, const float* l
   a.Hk = Hk;
   a.ld_head = (flags & DP_LA_HEAD_DECAY) != 0;
   a.qk_f32 = group || elem == 4;
-  a.sum_in_walk = !single && segments(L, a.geo.seg) <= kSumInBwd;
+  a.sum_in_walk = !single && sum_in_walk(s, a.geo, true);
   const hipStream_t st = static_cast<hipStream_t>(stream);
   hipError_t e = front(elem, s, a, single, 2, st);
   if (e == hipSuccess) e = stage(elem, dp::kLaBwd, a, dk, dv, 0, st);

@@ -623,6 +623,44 @@ def test_cuts(case, dtype):
         check(n, g[n], rg[n], low=dtype == "bf16" and n in "qkv")
 
 
+# B, H, Hk, L, dk, dv, decay, lens with many segments, on both sides of the rule for who adds
+# their states up: forwards and gradients of wide heads (the scan) and of narrow ones (the
+# walks, the decays' gradient too), of one length and packed with cut, uncut and empty
+# sequences side by side
+SIDES = [
+    (1, 4, 4, 2500, 128, 128, "token", None),
+    (2, 2, 1, 1300, 128, 64, "head", None),
+    (1, 2, 2, 2500, 32, 32, "token", None),
+    (1, 3, 1, 2000, 16, 64, "head", None),
+    (5, 2, 2, 2700, 128, 128, "token", [1700, 0, 40, 900, 60]),
+    (5, 3, 1, 2700, 128, 128, "head", [60, 900, 40, 0, 1700]),
+    (5, 2, 2, 2700, 64, 64, "head", [1700, 0, 40, 900, 60]),
+    (3, 2, 1, 1500, 32, 16, "token", [1400, 1, 99]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", SIDES, ids=[f"H{c[1]}-{c[2]}L{c[3]}d{c[4]}x{c[5]}{c[6]}{'p' if c[7] else ''}" for c in SIDES])
+def test_many_segments(case, dtype):
+    """Results against the definition, and the state passed on in one buffer, bit for bit
+    what two buffers give."""
+    B, H, Hk, L, dk, dv, decay, lens = case
+    x = make(B, H, Hk, L, dk, dv, dtype, decay, 3 * L + H, lens=lens)
+    say(f"case la many {case} {dtype}")
+    out, fs = run_fwd(x)
+    y = dev(x)
+    st = y["h0"].clone()
+    o, _ = dp.la_fwd(y["q"], y["k"], y["v"], y["ld"], cu_seqlens=y["cu"], h0=st, final_state=st)
+    torch.cuda.synchronize()
+    assert torch.equal(o, out) and torch.equal(st, fs)
+    g = run_bwd(x)
+    ro, rs, rg = reference(x, bwd=True)
+    check("out", out, ro, low=dtype == "bf16")
+    check("state", fs, rs)
+    for n in ("q", "k", "v", "h0", "ld"):
+        check(n, g[n], rg[n], low=dtype == "bf16" and n in "qkv")
+
+
 def test_calls_side_by_side():
     """Two streams with calls in flight at once, and two graphs of different inputs replayed
     on them together: each gives what it gives alone."""
