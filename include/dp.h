@@ -719,7 +719,8 @@ int dp_la_decode_bf16(const void* q, const void* k, const void* v, const float* 
  * input but x, and that only as the same buffer.
  *   x, gate, y [rows, G, D] T (gate nullable, not with DP_NORM_SILU; y MAY be x)
  *   weight, bias [G, D] f32, each nullable
- * Statistics and arithmetic in fp32, the result rounded once.  1 <= D <= 2048.
+ * Statistics and arithmetic in fp32 (rows whose sums or squares pass its range go through
+ * it scaled down), the result rounded once.  1 <= D <= 2048.
  * Errors: DP_EINVAL (null x or y with rows > 0, x, gate or y not 16-byte aligned,
  * sizes < 0, eps < 0 or NaN, an unknown flag), DP_ENOTSUP (D > 2048, rows G past
  * the 32-bit limit, G over 262140 or G D over 2^26 - 16), DP_EHIP.

@@ -162,7 +162,13 @@ struct NormRow {
 #pragma unroll
         for (int e = 0; e < N; ++e) s += f[e];
         s = norm_sum<LPR>(s);
-        const float m = pass == 0 ? s * inv : s / (float)D;
+        float m = pass == 0 ? s * inv : s / (float)D;
+        if (!__builtin_isfinite(s)) {  // values whose sum passes fp32's range: the sum of their D-ths
+          s = 0.f;
+#pragma unroll
+          for (int e = 0; e < N; ++e) s = fmaf(f[e], inv, s);
+          m = norm_sum<LPR>(s);
+        }
 #pragma unroll
         for (int e = 0; e < N; ++e) f[e] -= m;
         if (!full) {
@@ -171,17 +177,27 @@ struct NormRow {
         }
       }
     }
-    float q = 0.f;
+    auto squares = [&] {
+      float q = 0.f;
 #pragma unroll
-    for (int e = 0; e < N; ++e) q = fmaf(f[e], f[e], q);
+      for (int e = 0; e < N; ++e) q = fmaf(f[e], f[e], q);
+      return norm_sum<LPR>(q);
+    };
+    float q = squares(), down = 1.f;
+    if (__builtin_isinf(q)) {  // squares past fp32's range: of values 2^-80 as large, next to which eps is nothing
+      down = 0x1p-80f;
+#pragma unroll
+      for (int e = 0; e < N; ++e) f[e] *= down;
+      q = squares();
+    }
     // (the hardware's reciprocal root takes a denormal for zero: a spread below 1e-19 with
     // eps = 0 goes through it 2^64 times as large)
-    const float m2 = fmaf(norm_sum<LPR>(q), inv, eps);
+    const float m2 = fmaf(q, inv, down < 1.f ? 0.f : eps);
     const bool tiny = m2 < 0x1p-120f;
     const float r = __builtin_amdgcn_rsqf(tiny ? m2 * 0x1p64f : m2) * (tiny ? 0x1p32f : 1.f);
 #pragma unroll
     for (int e = 0; e < N; ++e) f[e] *= r;
-    return r;
+    return r * down;
   }
 };
 

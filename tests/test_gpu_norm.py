@@ -171,6 +171,31 @@ def test_tiny_spreads_without_eps(rms):
         assert float((y - want).abs().max()) <= 2.0 ** -15 * 2
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("D", [3, 64, 100, 2048])
+def test_large_values(D, rms, dtype):
+    """Rows whose squares (1e25) and whose sums (3e37 and an offset of 1e38) pass fp32's range
+    beside ordinary ones: the result has none of their size, and the gradient is 1 / spread of
+    it.  The mean of values on an offset is off by a few 2^-24 of the offset, here 3 times the
+    spread, and so is taken out: as in any row."""
+    gen = torch.Generator().manual_seed(D)
+    n = lambda *s: torch.randn(*s, generator=gen).clamp(-3, 3)
+    x, dy = n(6, 2, D), n(6, 2, D)
+    x[1] *= 1e25
+    x[3] = x[3] * 3e37 + (0 if rms else 1e38)
+    x[4] *= 1e19
+    x, dy = x.to(DT[dtype]), dy.to(DT[dtype])
+    y = dp.group_norm(x.cuda(), rms=rms)
+    g = dp.group_norm_bwd(x.cuda(), dy.cuda(), rms=rms)
+    torch.cuda.synchronize()
+    ry, rg, terms = reference(f64(x), None, None, None, f64(dy), 1e-5, rms, False)
+    for i in range(6):  # row by row: their gradients are of different sizes
+        check(f"y {i}", y[i], ry[i], dtype == "bf16")
+        if i != 3:  # 1 / 3e37 is a denormal's size
+            check(f"x {i}", g["x"][i], rg["x"][i], dtype == "bf16", terms[i])
+
+
 def test_saturated_gates():
     z = torch.tensor([-200.0, -90.0, -20.0, 0.0, 20.0, 90.0, 200.0, 1e30]).repeat(2).reshape(1, 1, 16)
     x = torch.arange(16.0).reshape(1, 1, 16)
