@@ -237,6 +237,22 @@ def test_in_place_streams_replays_and_empty():
     assert g["x"].shape == e.shape and bool((g["weight"] == 0).all()) and bool((g["bias"] == 0).all())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("G,D", [(5, 1), (3, 3), (7, 33), (12, 100), (2, 2047)])
+def test_in_place_at_odd_widths(G, D, dtype):
+    """y over x, dx over dy and the gate's gradient over the gate, where a group's last vector
+    is read from its neighbour channels and written by parts: the bits of separate buffers."""
+    gen = torch.Generator().manual_seed(D)
+    x, z, dy = (torch.randn(41, G, D, generator=gen).to(DT[dtype]).cuda() for _ in range(3))
+    w, b = torch.rand(G, D, generator=gen).cuda(), torch.rand(G, D, generator=gen).cuda()
+    for gate in (z, None):
+        y, g = dp.group_norm(x, w, b, gate, silu=gate is None), dp.group_norm_bwd(x, dy, w, b, gate, silu=gate is None)
+        xi, dyi, zi = x.clone(), dy.clone(), None if gate is None else gate.clone()
+        gi = dp.group_norm_bwd(x, dyi, w, b, zi, silu=gate is None, grads=dict(x=dyi) if gate is None else dict(x=dyi, gate=zi))
+        assert dp.group_norm(xi, w, b, gate, silu=gate is None, out=xi) is xi and torch.equal(xi, y)
+        assert set(gi) == set(g) and all(torch.equal(g[k], gi[k]) for k in g)
+
+
 def test_layer_linear_attention_norm_gate():
     """Linear attention, its norm with a SiLU gate, and the gradient through both, as a
     layer runs them, against fp64 autograd of the definition."""
