@@ -671,7 +671,9 @@ int dp_la_fwd_bf16(const void* q, const void* k, const void* v, const float* ld,
  *   dh0    [B, H, dk, dv]  f32   written, or NULL
  * Packed batches: the gradients of rows behind the last sequence are zero.
  * Sums run in a fixed order: the same call gives the same bits.  Nothing from a
- * forward call is needed.  workspace: dp_la_bwd_workspace_size() bytes.
+ * forward call is needed.  What is not finite in q, k, v or dout reaches, beside the
+ * gradients that depend on it, those of its head's other tokens in its chunk, and dld
+ * of its sequence.  workspace: dp_la_bwd_workspace_size() bytes.
  * No output overlaps an input.
  * Flags: 0 or DP_LA_HEAD_DECAY.  Errors: as dp_la_fwd_*, and DP_EINVAL for dld
  * without ld.

@@ -901,7 +901,7 @@ def la_fwd(q, k, v, ld=None, *, cu_seqlens=None, h0=None, out=None, final_state=
     rows behind its last entry are left as they were.  h0 [B,H,dk,dv] f32 (packed:
     [nseq,..]) or None.  out_dtype: the input dtype (default) or torch.float32.
     Returns (out [B,L,H,dv], final_state); final_state is None when return_state is
-    False and none was passed.
+    False and none was passed.  No graph is recorded: the gradient is :func:`la_bwd`.
     """
     lead, B, L, H, Hk, dk, dv, flags = _la_shapes(q, k, v, ld, cu_seqlens)
     dev, dt = q.device, q.dtype
@@ -935,8 +935,9 @@ def la_bwd(q, k, v, dout, ld=None, *, cu_seqlens=None, h0=None, dfinal=None, wor
     Inputs as :func:`la_fwd`, dout like v the gradient on out, dfinal [B,H,dk,dv] f32
     (or None) the gradient on the final state.  Returns a dict of gradients ``q, k,
     v`` in the inputs' dtype, ``h0`` f32 and, with log decays, ``ld`` f32 in their
-    shape; ``grads`` may hold preallocated tensors under those names.  Packed: rows
-    behind the last sequence get zeros.
+    shape; ``grads`` may hold preallocated tensors under those names, and None for
+    ``ld`` or ``h0`` leaves that one out (decays that are not trained: the products and
+    sums for their gradient are saved).  Packed: rows behind the last sequence get zeros.
     """
     lead, B, L, H, Hk, dk, dv, flags = _la_shapes(q, k, v, ld, cu_seqlens)
     dev, dt = q.device, q.dtype
@@ -1032,7 +1033,8 @@ def group_norm(x, weight=None, bias=None, gate=None, *, eps: float = 1e-5, rms: 
     x [..., G, D] (float32 or bfloat16): the D channels of every group are normalised
     on their own (rms: without the mean), scaled and shifted by weight, bias [G,D] f32,
     then passed through SiLU (silu) or multiplied by SiLU(gate) (gate like x).  The
-    out of :func:`fwd` and :func:`la_fwd` [B,L,H,dv] goes in as it is.
+    out of :func:`fwd` and :func:`la_fwd` [B,L,H,dv] goes in as it is.  No graph is
+    recorded: the gradient is :func:`group_norm_bwd`.
     """
     rows, G, D, flags = _norm_shapes(x, weight, bias, gate, rms, silu)
     suf = _suffix(x.dtype)
@@ -1059,7 +1061,8 @@ def group_norm_bwd(x, dy, weight=None, bias=None, gate=None, *, eps: float = 1e-
                    silu: bool = False, workspace=None, grads=None, stream=None) -> dict:
     """Gradient of :func:`group_norm` for a gradient dy on its result: a dict with
     ``x``, and ``weight``, ``bias`` (f32) and ``gate`` for those that were given;
-    ``grads`` may hold preallocated tensors under those names."""
+    ``grads`` may hold preallocated tensors under those names, and None for ``weight``
+    or ``bias`` leaves that one out."""
     rows, G, D, flags = _norm_shapes(x, weight, bias, gate, rms, silu)
     dev, suf = x.device, _suffix(x.dtype)
     _need(dy, "dy", x.dtype, x.shape, dev)
@@ -1110,8 +1113,9 @@ def state_copy(pool, src, dst, *, stream=None) -> None:
 class StatePool:
     """A pool of recurrent states [layers, nslots, H, dk, dv] (fp32) and the host's
     list of its free slots: what a serving loop keeps around :func:`la_decode` (its
-    `slots`) or :func:`decode`.  Slots are handed out lowest first; `stream` as for
-    :func:`state_copy`."""
+    `slots`).  :func:`decode` takes no slots: it runs on ``states[l, :n]`` when the
+    sequences are slots 0 .. n - 1, as after :meth:`compact`.  Slots are handed out
+    lowest first; `stream` as for :func:`state_copy`."""
 
     def __init__(self, layers, nslots, H, dk, dv, device="cuda"):
         if min(layers, nslots, H, dk, dv) < 1:

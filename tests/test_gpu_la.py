@@ -366,7 +366,9 @@ def test_results_do_not_depend_on_what_else_is_asked_for(case):
     g = run_bwd(x)
     for left in (["ld"], ["h0"], ["ld", "h0"]):
         part = run_bwd(x, grads={n: None for n in left})
-        assert all(torch.equal(g[n], part[n]) for n in g if n not in left), left
+        assert all(part[n] is None if n in left else torch.equal(g[n], part[n]) for n in g), left
+    with pytest.raises(dp.DPError):
+        run_bwd(x, grads=dict(q=None))
 
 
 @pytest.mark.parametrize("case", ASKED, ids=[f"B{c[0]}H{c[1]}L{c[3]}d{c[4]}x{c[5]}" for c in ASKED])

@@ -237,6 +237,18 @@ def test_in_place_streams_replays_and_empty():
     assert g["x"].shape == e.shape and bool((g["weight"] == 0).all()) and bool((g["bias"] == 0).all())
 
 
+def test_gradients_left_out():
+    gen = torch.Generator().manual_seed(8)
+    x, z, dy = (torch.randn(50, 4, 64, generator=gen).cuda() for _ in range(3))
+    w, b = torch.rand(4, 64, generator=gen).cuda(), torch.rand(4, 64, generator=gen).cuda()
+    g = dp.group_norm_bwd(x, dy, w, b, z)
+    for left in (["weight"], ["bias"], ["weight", "bias"]):
+        part = dp.group_norm_bwd(x, dy, w, b, z, grads={n: None for n in left})
+        assert all(part[n] is None if n in left else torch.equal(g[n], part[n]) for n in g)
+    with pytest.raises(dp.DPError):
+        dp.group_norm_bwd(x, dy, w, b, z, grads=dict(x=None))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("G,D", [(5, 1), (3, 3), (7, 33), (12, 100), (2, 2047)])
 def test_in_place_at_odd_widths(G, D, dtype):
