@@ -508,10 +508,11 @@ __device__ __forceinline__ int la_here(int x) {
 // them: all share the loads and the scores, the columns of a narrow head belong to the
 // first dv / 16.  A chunk is a chain of short steps, so its time on an idle CU is issue
 // and latency of one wavefront: with eight, each holds half as much.  The forward takes
-// eight where dv = 128 fills them (B = 16, H = 16, L = 1024, d = 128: 85 us with one
-// workgroup a CU against 111 with two of four wavefronts and twice the segments; 512
-// tokens of 8 heads 18 against 21).  The gradient keeps two workgroups of four, whose
-// reads of the shared rows are fewer (366 against 390 us at B = 4, H = 16, L = 4096).
+// eight where dv = 128 fills them (B = 16, H = 16, L = 1024, d = 128: 87 us with one
+// workgroup a CU against 114 with two of four wavefronts and twice the segments; 512
+// tokens of 8 heads 17.6 against 20.7).  The gradient keeps two workgroups of four, whose
+// reads of the shared rows are fewer (B = 4, H = 16, d = 128: L = 2048 190 against 203
+// us, L = 4096 395 against 386; d = 64, L = 4096 180 against 230; fp32 406 against 459).
 constexpr int la_fwd_waves(int dv) { return dv == 128 ? 8 : 4; }
 constexpr int kLaBwdWaves = 4;
 constexpr int la_waves(int dv, int nw) { return dv / 16 < nw ? dv / 16 : nw; }

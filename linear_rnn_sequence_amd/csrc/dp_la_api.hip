@@ -61,13 +61,12 @@ int check_grid(const LaShape& s, const dp::LaGeo& g) {
 
 // Segments: about `target` workgroups in all, of `least` chunks of 64 tokens at least.
 // More segments give a short batch the whole chip (a workgroup walks its chunks one
-// after another, 2 to 5 us each); each costs its state (dk dv fp32) being written,
-// summed and read again, and the states' pass reads two tensors a second time.  So a
-// batch whose heads alone fill the chip is not cut, nor a sequence of kAlone tokens, for
-// which one launch is quicker than two (256 tokens of 8 heads of 64: 12.4 against 16.4 us).
-constexpr int kAlone = 256;
+// after another, 2 to 5 us each, fp32 3 to 13); each costs its state (dk dv fp32) being
+// written, summed and read again, and the states' pass reads two tensors a second time.
+// So a batch whose heads alone fill the chip is not cut, nor a sequence of `alone` chunks,
+// for which one launch is quicker than two.
 int segments(int L, int seg) { return (int)(((long long)L + seg - 1) / seg); }
-void plan(const LaShape& s, int target, int least, dp::LaGeo* g, int* single) {
+void plan(const LaShape& s, int target, int least, int alone, dp::LaGeo* g, int* single) {
   const long long chunks = (s.rows() + kChunk - 1) / kChunk;
   long long segs = (target + s.H - 1) / s.H;  // wanted over all sequences
   if (segs < s.B) segs = s.B;
@@ -78,7 +77,7 @@ void plan(const LaShape& s, int target, int least, dp::LaGeo* g, int* single) {
     const long long c = segments(s.L, kChunk), n = segs / s.B;
     per = (c + n - 1) / n;
   }
-  if (s.L <= kAlone) per = kAlone / kChunk;
+  if (segments(s.L, kChunk) <= alone) per = alone;
   if (per < least) per = least;
   g->nseq = s.B;
   g->L = s.L;
@@ -88,13 +87,23 @@ void plan(const LaShape& s, int target, int least, dp::LaGeo* g, int* single) {
   // packed: sum over sequences of max(1, ceil(len / seg)) <= nseq + L / seg
   g->nwork = s.packed ? s.B + s.L / g->seg : s.B * g->nps;  // no more than rows / 64 + B
 }
-// Forward: one workgroup of eight wavefronts a CU, or two of four.  Gradient: three roles
-// of one workgroup a CU, and two chunks a segment at least (8 heads of 2048 tokens:
-// 47 against 59 us with one).
+// Forward: one workgroup of eight wavefronts a CU, or two of four.  A second launch and its
+// workspace cost the host 4 us and the GPU 2: a sequence is walked alone for two chunks, and
+// for three where a narrow state makes them short (8 heads, alone against cut, as the GPU
+// runs them and as calls of one stream, which the host bounds: bf16 d = 128, 128 tokens
+// 12.8 / 13.9 and 12.8 / 16.3 us, 256 tokens 22.1 / 15.1 and 22.2 / 16.3; d = 64, 192
+// tokens 11.0 / 10.1 and 11.8 / 16.2, 256 tokens 13.6 / 10.6 and 13.9 / 16.3; fp32 d = 64,
+// 192 tokens 17.7 / 13.2 and 17.8 / 16.2, 256 tokens 22.5 / 13.7 and 22.6 / 16.2, d = 128,
+// 128 tokens 28.4 / 24.9, 256 tokens 53 / 26).  Types share the rule, as they share the
+// workspace's size.
+// Gradient: three roles of one workgroup a CU, two chunks a segment at least (8 heads of
+// 128, 2048 tokens: 48 against 61 us with one), and four alone: 192 tokens are quicker so
+// everywhere (8 heads of 128 28 / 34 us, 64 of them 30 / 40), 256 where heads are many
+// and wide (64 of 128 38 / 42 us, 64 of 64 25.6 / 23.4, 8 of 128 36 / 34).
 void plan_fwd(const LaShape& s, dp::LaGeo* g, int* single) {
-  plan(s, dp::la_fwd_waves(s.dv) == 8 ? 256 : 512, 1, g, single);
+  plan(s, dp::la_fwd_waves(s.dv) == 8 ? 256 : 512, 1, s.dk * s.dv <= 64 * 64 ? 3 : 2, g, single);
 }
-void plan_bwd(const LaShape& s, dp::LaGeo* g, int* single) { plan(s, 256, 2, g, single); }
+void plan_bwd(const LaShape& s, dp::LaGeo* g, int* single) { plan(s, 256, 2, 4, g, single); }
 // Whether the walks add up the earlier segments' states themselves or start from the scan's
 // sums, by what either costs a sequence of n segments, in microseconds (fp32 states either
 // way, so the inputs' type does not matter):

@@ -1,6 +1,6 @@
 """Build the fp64 CPU oracle (``liboracle.so``) with gcc.
 
-Test infrastructure only: the library this builds is the checker, never part
+Test infrastructure only: the library this builds is the oracle, never part
 of the product path.
 """
 import os

@@ -642,6 +642,21 @@ SIDES = [
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_lengths_around_the_first_cut(d, dtype):
+    """Walked alone, and cut into segments of a chunk."""
+    for L in (128, 129, 192, 193, 256, 257):
+        x = make(1, 2, 1, L, d, d, dtype, "token", L)
+        out, fs = run_fwd(x)
+        g = run_bwd(x)
+        ro, rs, rg = reference(x, bwd=True)
+        check(f"out {L}", out, ro, low=dtype == "bf16")
+        check(f"state {L}", fs, rs)
+        for n in ("q", "k", "v", "h0", "ld"):
+            check(f"{n} {L}", g[n], rg[n], low=dtype == "bf16" and n in "qkv")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("case", SIDES, ids=[f"H{c[1]}-{c[2]}L{c[3]}d{c[4]}x{c[5]}{c[6]}{'p' if c[7] else ''}" for c in SIDES])
 def test_many_segments(case, dtype):
     """Results against the definition, and the state passed on in one buffer, bit for bit

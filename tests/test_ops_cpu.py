@@ -94,6 +94,13 @@ def test_linear_attention_workspace_sizes(lib):
     assert lib.dp_la_bwd_workspace_size(1, 1, 1, 1, 16, 17, 0, ctypes.byref(out)) == E.DP_ENOTSUP
 
 
+def test_short_sequences_are_not_cut(lib):
+    """Alone up to two chunks of a wide state, three of a narrow one; cut ones need states."""
+    for d, alone in ((128, 128), (64, 192), (16, 192)):
+        assert dp.la_fwd_workspace_size(1, 8, 8, alone, d, d) == 0
+        assert dp.la_fwd_workspace_size(1, 8, 8, alone + 1, d, d) >= 2 * 8 * d * d * 4
+
+
 def test_longest_sequences_are_cut_as_short_ones(lib):
     """Two thousand million tokens of a head: a state and a decay per segment, about as
     many segments as for a tenth of them (a length near 2^31 plus a segment passes 32 bits)."""
