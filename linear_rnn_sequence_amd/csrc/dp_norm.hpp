@@ -185,7 +185,7 @@ struct NormRow {
       return norm_sum<LPR>(q);
     };
     float q = squares(), down = 1.f;
-    if (__builtin_isinf(q)) {  // squares past fp32's range: of values 2^-80 as large, next to which eps is nothing
+    if (__builtin_isinf(q)) {  // squares past fp32's range: of values 2^-80 as large
       down = 0x1p-80f;
 #pragma unroll
       for (int e = 0; e < N; ++e) f[e] *= down;
@@ -193,7 +193,7 @@ struct NormRow {
     }
     // (the hardware's reciprocal root takes a denormal for zero: a spread below 1e-19 with
     // eps = 0 goes through it 2^64 times as large)
-    const float m2 = fmaf(q, inv, down < 1.f ? 0.f : eps);
+    const float m2 = fmaf(q, inv, eps * down * down);
     const bool tiny = m2 < 0x1p-120f;
     const float r = __builtin_amdgcn_rsqf(tiny ? m2 * 0x1p64f : m2) * (tiny ? 0x1p32f : 1.f);
 #pragma unroll

@@ -196,6 +196,13 @@ def test_large_values(D, rms, dtype):
             check(f"x {i}", g["x"][i], rg["x"][i], dtype == "bf16", terms[i])
 
 
+def test_large_values_and_eps():
+    """An eps next to squares past fp32's range (2^128) counts as next to smaller ones."""
+    x = torch.randn(4, 2, 64, generator=torch.Generator().manual_seed(5)) * 3e19
+    y = dp.group_norm(x.cuda(), eps=1e38)
+    check("y", y, reference(f64(x), None, None, None, np.zeros(x.shape), 1e38, False, False)[0], False)
+
+
 def test_saturated_gates():
     z = torch.tensor([-200.0, -90.0, -20.0, 0.0, 20.0, 90.0, 200.0, 1e30]).repeat(2).reshape(1, 1, 16)
     x = torch.arange(16.0).reshape(1, 1, 16)
