@@ -24,8 +24,10 @@
 //
 // The gradient of the log decay, dl_t = <D_t, e^{l_t} S_{t-1}>, needs no division by the
 // decay.  Take apart q_i . dq_i = a_i + r_i and k_j . dk_j = b_j + c_j into the state's
-// part and the scores' part.  Pairs (i, j) of one chunk with i >= t > j give the suffix
-// sums of r - c inside the chunk; everything that crosses the chunk's borders gives
+// part and the scores' part.  Pairs (i, j) of one chunk with i >= t > j give the sums of
+// r - c from t to the chunk's end, or those of c - r before t, the same number: the shorter
+// sum is taken (none at a chunk's first token, so that the first one of a sequence without
+// an initial state gets exactly 0); everything that crosses the chunk's borders gives
 // F - sum_{i < t} a_i + sum_{j < t} b_j, where F = <S, D> at the segment's start and the
 // sums run from there.  (Summing q . dq - k . dk alone, from the segment's end, is the
 // same number, but its rounding grows with the segment where the true value is as small

@@ -120,8 +120,9 @@ static __global__ __launch_bounds__(256) void dp_la_scan_kernel(LaArgs p, int pe
 }
 
 // dl of one segment and head (see the head of dp_la.hpp): <S, D> at the segment's start,
-// plus the sums of b - a from there to before the token, plus the suffix sums of r - c
-// inside the token's chunk of C, all in fp64.  A decay that erases the state has gradient
+// plus the sums of b - a from there to before the token, plus what the token's chunk of C
+// adds: the sums of c - r before it, in the chunk's second half those of r - c from it on,
+// all in fp64.  A decay that erases the state has gradient
 // zero (the difference of the sums would leave their rounding).  With one decay per head
 // the segment's sum of dl goes to ldpart.
 constexpr int kDldThreads = 512;
@@ -205,15 +206,16 @@ __global__ __launch_bounds__(kDldThreads) void dp_la_dld_kernel(LaArgs p, int pe
     if (e + NT < sg.len) fetch(e + NT);
     const double cc = la_scan64(cross), ci = la_scan64(in);
     if (l == 63) run[wave] = cc;
-    // the chunk's total of r - c: lane 63's, or for chunks of 32 lane 31's and the rest
+    // the sums of r - c up to the chunk's start and its end, which lanes 31 and 63 hold
     const double t0 = __shfl(ci, C - 1), t1 = __shfl(ci, 63);
-    const double suffix = (C == 64 || l < 32 ? t0 : t1) - ci + in;
+    const bool lower = C == 64 || l < 32;
+    const double inside = ((l & (C - 1)) < C / 2 ? (lower ? 0.0 : t0) : (lower ? t0 : t1)) - ci + in;
     __syncthreads();
     double before = carry + cc - cross;
     for (int w = 0; w < wave; ++w) before += run[w];
     const int i = e + tid;
     if (i < sg.len) {
-      const double d = erases ? 0.0 : before + suffix;
+      const double d = erases ? 0.0 : before + inside;
       sum += d;
       if (!p.ld_head) p.dld[(sg.row + i) * p.H + h] = (float)d;
     }

@@ -288,6 +288,35 @@ def test_gradient_of_an_erasing_decay_is_zero(case, dtype):
         check(n, g[n], rg[n], low=dtype == "bf16" and n in "qkv")
 
 
+# sequences without an initial state: B, H, Hk, L, dk, dv, decay, lens; single tokens, a few,
+# one and many segments
+FIRST = [(5, 2, 1, 1, 128, 32, "token", None), (3, 4, 2, 1, 64, 64, "head", None), (2, 2, 2, 3, 32, 128, "token", None),
+         (2, 2, 2, 700, 64, 64, "token", None), (6, 2, 2, 300, 16, 64, "token", [1, 0, 1, 270, 2, 26])]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", FIRST, ids=[f"B{c[0]}L{c[3]}d{c[4]}{c[6]}{'p' if c[7] else ''}" for c in FIRST])
+def test_gradient_of_the_first_decay(case, dtype):
+    """Nothing precedes a sequence's first token, so its decay's gradient is exactly zero, with
+    one decay per head also the sum over sequences of a token; with an initial state it is
+    e^ld <h0, D>, to an fp32 product's error of itself where it is the only token."""
+    B, H, Hk, L, dk, dv, decay, lens = case
+    x = make(B, H, Hk, L, dk, dv, dtype, decay, 71 + L, lens=lens, h0=False)
+    g = run_bwd(x)
+    rg = reference(x, bwd=True)[2]
+    if decay == "head":
+        assert bool((g["ld"] == 0).all())
+    else:
+        at = g["ld"][:, 0] if lens is None else g["ld"][[int(c) for c, n in zip(x["cu"], lens) if n]]
+        assert bool((at == 0).all())
+    for n in ("q", "k", "v", "ld"):
+        check(n, g[n], rg[n], low=dtype == "bf16" and n in "qkv")
+    if L == 1:
+        y = make(B, H, Hk, L, dk, dv, dtype, decay, 73, h0=True)
+        y["h0"] *= 1e-3
+        check("ld", run_bwd(y)["ld"], reference(y, bwd=True)[2]["ld"])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_gradient_against_differences(dtype):
     """Directional derivatives of the fp64 definition by central differences."""
