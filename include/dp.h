@@ -665,9 +665,9 @@ int dp_la_fwd_bf16(const void* q, const void* k, const void* v, const float* ld,
  *   dv_out [B, L, H, dv]   T     written
  *   dld    [B, L, H] f32 ([H] with DP_LA_HEAD_DECAY: summed over all tokens), or
  *                                NULL (not returned); needs ld.  Zero where ld <= -1000
- *                                erases the state; else exact to fp32 rounding of the
- *                                q . dq and k . dk around the token, not of itself: a
- *                                strong decay's tiny gradient can be less than that
+ *                                erases the state; else off by an fp32 rounding of the
+ *                                sequence's gradients around it, not of itself: next to
+ *                                weak decays a strong one's can be less than that
  *   dh0    [B, H, dk, dv]  f32   written, or NULL
  * Packed batches: the gradients of rows behind the last sequence are zero.
  * Sums run in a fixed order: the same call gives the same bits.  Nothing from a

@@ -23,13 +23,15 @@
 // j >= i).  LaWalk below is that walk.
 //
 // The gradient of the log decay, dl_t = <D_t, e^{l_t} S_{t-1}>, needs no division by the
-// decay.  Take apart q_i . dq_i = a_i + r_i and k_j . dk_j = b_j + c_j into the state's
-// part and the scores' part.  Pairs (i, j) of one chunk with i >= t > j give the sums of
-// r - c from t to the chunk's end, or those of c - r before t, the same number: the shorter
-// sum is taken (none at a chunk's first token, so that the first one of a sequence without
-// an initial state gets exactly 0); everything that crosses the chunk's borders gives
-// F - sum_{i < t} a_i + sum_{j < t} b_j, where F = <S, D> at the segment's start and the
-// sums run from there.  (Summing q . dq - k . dk alone, from the segment's end, is the
+// decay.  Take apart q_i . dq_i = a_i + r_i + o_i and k_j . dk_j = b_j + c_j + o_j into the
+// state's part, the scores' part of other tokens and that of the token itself (which is
+// the same for both and cancels: left in, it leaves its rounding in the gradient of short
+// or quickly forgetting sequences, where it is the largest term).  Pairs (i, j) of one
+// chunk with i >= t > j give the sums of r - c from t to the chunk's end, or those of c - r
+// before t, the same number: the shorter sum is taken (none at a chunk's first token, so
+// that the first one of a sequence without an initial state gets exactly 0); everything
+// that crosses the chunk's borders gives F - sum_{i < t} a_i + sum_{j < t} b_j, where F =
+// <S, D> at the segment's start and the sums run from there.  (Summing q . dq - k . dk alone, from the segment's end, is the
 // same number, but its rounding grows with the segment where the true value is as small
 // as one token's terms; a and b shrink with the decay and take their rounding along.)
 //
@@ -631,7 +633,8 @@ __device__ __forceinline__ float la_dot(const u32x4_t (&q)[CT], const f32x4_t (&
 struct LaWalkArgs {
   LaTen a, b, c;      // rows, columns [.., DK] and values [.., DV]
   LaTen dot;          // rows [.., DV] whose products with the result rows are wanted, or null
-  float2* dots;       // [row][H]: with the state's part of the result row, with the scores' part
+  float2* dots;       // [row][H]: with the state's part of the result row, with the scores' part (`apart`: i != j)
+  int apart;          // each token's own score goes into its row after the products with `dot`
   void* r;            // result [row][H][DV], T or fp32
   const float* ld;    // log decays, or null
   int ld_head;        // one per head ([H]) instead of [row][H]
@@ -657,14 +660,16 @@ struct LaWalk {
   static constexpr int oC = oB + C * LA * (int)sizeof(T);
   static constexpr int oP = oC + C * LC * (int)sizeof(T);
   static constexpr int oG = oP + NS * C * LP * (int)sizeof(T);
-  static constexpr int oDot = oG + 4 * LaDecayRing<C>::BYTES;
-  static constexpr int LDS = oDot, LDS_DOTS = oDot + WV * C * 8;  // without and with products (`dots`)
+  static constexpr int oOwn = oG + 4 * LaDecayRing<C>::BYTES;
+  static constexpr int oDot = oOwn + C * 4;
+  static constexpr int LDS = oOwn, LDS_DOTS = oDot + WV * C * 8;  // without and with `apart` and `dots`
 
   __device__ __forceinline__ static void run(const LaWalkArgs& p, char* lds, long long row0, int len, int h) {
     T* sA = reinterpret_cast<T*>(lds + oA);
     T* sB = reinterpret_cast<T*>(lds + oB);
     T* sC = reinterpret_cast<T*>(lds + oC);
     T* sP = reinterpret_cast<T*>(lds + oP);
+    float* sOwn = reinterpret_cast<float*>(lds + oOwn);
     float2* sDot = reinterpret_cast<float2*>(lds + oDot);
     const int tid = threadIdx.x, l = tid & 63, g = l >> 4, n = l & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -771,12 +776,15 @@ struct LaWalk {
       for (int u = 0; u < NTL; ++u) {
         const double gi = sG[16 * rt[u] + n];
         const double* gj = sG + 16 * ct[u] + 4 * g;
-        const int edge = 16 * (rt[u] - ct[u]) + n - 4 * g;  // forwards j <= i: e <= edge
+        const int edge = 16 * (rt[u] - ct[u]) + n - 4 * g;  // j = i: e = edge; forwards j <= i: e <= edge
+        const int last = rev ? edge + p.apart : edge - p.apart;
+        if (p.apart && rt[u] == ct[u] && n >> 2 == g)
+          sOwn[16 * rt[u] + n] = n & 2 ? (n & 1 ? sc[u][3] : sc[u][2]) : (n & 1 ? sc[u][1] : sc[u][0]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float d = rev ? (float)(gj[e] - gi) : (float)(gi - gj[e]);
           const float v = sc[u][e] * __builtin_amdgcn_exp2f(d);
-          sc[u][e] = (rev ? e >= edge : e <= edge) ? v : 0.f;
+          sc[u][e] = (rev ? e >= last : e <= last) ? v : 0.f;
         }
         Op::template put<NS>(sP + 16 * rt[u] * LP + Op::pcol_step(rp0, ct[u]), C * LP, sc[u]);
       }
@@ -836,7 +844,25 @@ struct LaWalk {
             }
           }
         }
-        // write the rows, and their products with the rows of `dot`
+        // the rows' products with those of `dot`, then each token's own score times its values
+        if (p.dots != nullptr) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float all = la_dot<Op, CT>(dq[r], acc[r]);
+            if (g == 0) sDot[wave * C + 16 * r + n] = float2{ds[r], all - ds[r]};
+          }
+        }
+        if (p.apart) {
+          const int ov = la_here(Op::row_lane(LC));
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float own = sOwn[16 * r + n];
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+              acc[r][t] += Op::widen4(Op::load4(sC + 16 * r * LC + Op::tr_step(ov, col0 / 16 + t))) * own;
+          }
+        }
+        // write the rows
         const int ro = n * p.H * DV + col0 + 4 * g;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -850,10 +876,6 @@ struct LaWalk {
               else
                 Op::template put<1>(static_cast<T*>(p.r) + o + (ro + 16 * t), 0, acc[r][t]);
             }
-          }
-          if (p.dots != nullptr) {
-            const float all = la_dot<Op, CT>(dq[r], acc[r]);
-            if (g == 0) sDot[wave * C + 16 * r + n] = float2{ds[r], all - ds[r]};
           }
         }
         if (it + 1 < nc || p.x1 != nullptr)
@@ -1062,6 +1084,7 @@ __global__ __launch_bounds__(64 * kLaBwdWaves, 2) void dp_la_bwd_kernel(LaArgs p
     w.c = role == 0 ? k : q;
     w.r = role == 0 ? p.dq : p.dk;
     w.r_f32 = p.qk_f32;
+    w.apart = 1;  // whether the decays' gradient is asked for or not: the same bits
     w.dot = role == 0 ? q : k;
     w.dots = role == 0 ? p.xq : p.xk;
   }

@@ -317,6 +317,22 @@ def test_gradient_of_the_first_decay(case, dtype):
         check("ld", run_bwd(y)["ld"], reference(y, bwd=True)[2]["ld"])
 
 
+# B, H, Hk, L, dk, dv, decay, lens: two to ten tokens, decays down to e^-20, no initial state
+SHORT = [(1, 1, 1, 2, 64, 64, "strong", None), (4, 1, 1, 6, 32, 128, "strong", [0, 2, 0, 4]), (6, 4, 2, 2, 64, 64, "strong", None),
+         (3, 4, 4, 5, 128, 16, "strong", None), (5, 4, 1, 30, 16, 32, "strong", [2, 10, 3, 15, 0]), (3, 8, 8, 3, 128, 128, "head", None)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", SHORT, ids=[f"B{c[0]}L{c[3]}d{c[4]}{c[6]}{'p' if c[7] else ''}" for c in SHORT])
+def test_decay_gradient_of_short_sequences(case, dtype):
+    """Only pairs of different tokens enter it, far smaller than a token's own term when they
+    are few or the decays strong: an fp32 result's error relative to itself all the same."""
+    B, H, Hk, L, dk, dv, decay, lens = case
+    for seed in range(5):
+        x = make(B, H, Hk, L, dk, dv, dtype, decay, 79 + seed, lens=lens, h0=False)
+        check("ld", run_bwd(x)["ld"], reference(x, bwd=True)[2]["ld"])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_gradient_against_differences(dtype):
     """Directional derivatives of the fp64 definition by central differences."""
