@@ -668,6 +668,7 @@ int dp_la_fwd_bf16(const void* q, const void* k, const void* v, const float* ld,
  *                                erases the state; else off by an fp32 rounding of the
  *                                sequence's gradients around it, not of itself: next to
  *                                weak decays a strong one's can be less than that
+ *                                (and with DP_LA_HEAD_DECAY a sum that cancels)
  *   dh0    [B, H, dk, dv]  f32   written, or NULL
  * Packed batches: the gradients of rows behind the last sequence are zero.
  * Sums run in a fixed order: the same call gives the same bits.  Nothing from a

@@ -1021,7 +1021,7 @@ __device__ __forceinline__ void la_end(const LaArgs& p, const LaSeg& sg, int s, 
 }
 
 // The forward walk: one workgroup per segment and head.  B = 4, H = 16, L = 4096, d = 128:
-// the call takes 122 to 127 us (traced, at lower clocks, this kernel 102 to 119 and the
+// the call takes 122 to 128 us (traced, at lower clocks, this kernel 102 to 120 and the
 // states 39 to 47), 16 chunks a workgroup; bound by the issue of its products (64 GFLOP
 // with the terms, 51 us at the 1.27 PFLOP/s of a large library product) and of the
 // exponentials, splits and LDS reads between them, which overlap in part.
@@ -1049,8 +1049,8 @@ __global__ __launch_bounds__(64 * la_fwd_waves(DV), 2) void dp_la_fwd_kernel(LaA
 
 // The gradient's walks, one workgroup per segment, head and role: dq (forwards
 // over the transposed state), dk (backwards, transposed) and dv (backwards).  B = 4, H =
-// 16, L = 4096, d = 128, with the decays' gradient: the call takes 383 to 404 us (traced,
-// this kernel 322 to 345), bound as the forward: 245 GFLOP in all, 193 us at that rate.
+// 16, L = 4096, d = 128, with the decays' gradient: the call takes 388 to 404 us (traced,
+// this kernel 339 to 355), bound as the forward: 245 GFLOP in all, 193 us at that rate.
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__(64 * kLaBwdWaves, 2) void dp_la_bwd_kernel(LaArgs p) {
   extern __shared__ __align__(16) char lds[];
